@@ -259,6 +259,9 @@ __global__ void __launch_bounds__(NT * G, C <= 2 ? 3 : 2) backward_kernel(const 
         unpack<T>(cur.dy[c], y);
         unpack<T>(cur.h[c], x);
         if constexpr (!HOLD) {
+          // dx may be dh itself, and its other chunks have been stored by now: only
+          // a chunk's own thread reads it here
+          if (c * NT + tid >= whole) continue;
           gv[0] = has_dh ? load_at(dhrow(row), at(c)) : u32x4{0u, 0u, 0u, 0u};
           load_weights<CE>(a.w, a.w_dtype, (int)(at(c) / ESZ), n, wc);
         }

@@ -89,7 +89,9 @@ __device__ __forceinline__ u32x4 pack(const float (&f)[16 / Elem<T>::size]) {
 // thread past the end takes the last chunk: it loads it and stores the
 // same result as the chunk's own thread, and only the sums leave it out.  So the
 // passes over a row have no branch, which lets the compiler count the loads in
-// flight instead of waiting for all of them.
+// flight instead of waiting for all of them.  This holds for what is loaded before
+// any of the row's stores: where an output takes an input's place, a pass that
+// loads between its stores leaves these threads out.
 template <int NT>
 __device__ __forceinline__ uint32_t chunk_offset(int c, int t, int whole) {
   const int i = c * NT + t;

@@ -1,0 +1,92 @@
+"""The row operators of the training block (norm and distillation) where an
+output takes an input's place, over more rows than workgroups, and at the
+limits of row counts and pitches.
+
+Tolerances are those of test_gpu_train.py.  An operator in place is compared
+bit by bit with the same call out of place: it does the same arithmetic.
+"""
+
+import pytest
+import torch
+
+import train_reference as R
+from gpu_util import announce, require_gpu
+from test_gpu_train import DT, U, normal, row_tol
+
+pytestmark = pytest.mark.gpu
+
+
+def c_call(fn, t, *args):
+    """fn of the C ABI on t's device and its current stream; tensors are passed
+    by address."""
+    from msign_newton_schulz_amd import _train
+    args = [a.data_ptr() if isinstance(a, torch.Tensor) else a for a in args]
+    _train._launch(t.device, getattr(_train._library(), fn), *args)
+
+
+DTYPE = {"f32": 0, "bf16": 1, "f16": 2}
+
+# Each configuration of both passes (by the 16-byte chunks of a row), at widths
+# whose chunks do not fill its threads, and full ones.
+WIDTHS = [("bf16", 2000, 96), ("bf16", 5000, 500), ("bf16", 2000, 1000), ("f16", 1100, 2003), ("bf16", 1100, 4001),
+          ("bf16", 800, 6001), ("f16", 800, 8100), ("bf16", 300, 16001), ("bf16", 300, 16392), ("bf16", 300, 17001),
+          ("bf16", 300, 20000), ("f16", 300, 24000), ("bf16", 5, 32768), ("f32", 5000, 250), ("f32", 2000, 500),
+          ("f32", 1100, 2001), ("f32", 800, 3001), ("f32", 800, 4001), ("f32", 300, 8001), ("f32", 300, 8196),
+          ("f32", 300, 9001), ("f32", 300, 12288), ("f32", 300, 20001), ("f32", 5, 32768)]
+
+
+@pytest.mark.parametrize("kind,rows,dim", WIDTHS)
+def test_norm_backward_in_place(kind, rows, dim):
+    """dx in the place of dy, of dh, and of both where they are one tensor."""
+    M = require_gpu()
+    dy, dh, h = (normal((rows, dim), 1.0, kind, 1 + i) for i in range(3))
+    w = normal((dim,), 0.2, kind, 4) + 1
+    rstd = (h.double().square().mean(1) + 1e-6).rsqrt().float()
+    ws = torch.empty(768 * dim * 4 + 256, dtype=torch.uint8, device="cuda")
+
+    def run(dy, dh, dx):
+        dw = torch.empty_like(w)
+        c_call("add_rms_norm_backward", h, dy, dim, h, dim, rstd, w, dh, dim, dx, dw, rows, dim, DTYPE[kind],
+               DTYPE[kind], ws, ws.numel())
+        return dw
+
+    announce(f"norm backward in place {rows} {dim} {kind}")
+    want = M.add_rms_norm_backward(dy, h, rstd, w, dh=dh)
+    for place in ("dy", "dh"):
+        a, b = dy.clone(), dh.clone()
+        dx = a if place == "dy" else b
+        dw = run(a, b, dx)
+        torch.cuda.synchronize()
+        assert torch.equal(dx, want[0]) and torch.equal(dw, want[1]), place
+    want = M.add_rms_norm_backward(dy, h, rstd, w, dh=dy)
+    dx = dy.clone()
+    dw = run(dx, dx, dx)
+    torch.cuda.synchronize()
+    assert torch.equal(dx, want[0]) and torch.equal(dw, want[1])
+
+
+@pytest.mark.parametrize("kind,rows,dim", WIDTHS)
+def test_norm_forward_in_place(kind, rows, dim):
+    """h_out in the place of x, of the residual, and of both where they are one
+    tensor."""
+    M = require_gpu()
+    x, r = normal((rows, dim), 1.0, kind, 5), normal((rows, dim), 2.0, kind, 6)
+    w = normal((dim,), 0.2, kind, 7) + 1
+
+    def run(x, r, h):
+        y, rstd = torch.empty_like(x), torch.empty(rows, device="cuda")
+        c_call("add_rms_norm", x, x, dim, r, dim, w, y, h, rstd, rows, dim, DTYPE[kind], DTYPE[kind], 1e-6)
+        return y, h, rstd
+
+    announce(f"norm forward in place {rows} {dim} {kind}")
+    want = M.add_rms_norm(x, w, r)
+    for place in ("x", "residual"):
+        a, b = x.clone(), r.clone()
+        got = run(a, b, a if place == "x" else b)
+        torch.cuda.synchronize()
+        assert all(torch.equal(p, q) for p, q in zip(got, want)), place
+    want = M.add_rms_norm(x, w, x)
+    a = x.clone()
+    got = run(a, a, a)
+    torch.cuda.synchronize()
+    assert all(torch.equal(p, q) for p, q in zip(got, want))
