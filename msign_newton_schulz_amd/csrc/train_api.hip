@@ -235,6 +235,9 @@ bool matrix_ok(const void* p, int64_t rows, int64_t cols, int64_t ld, int64_t si
   return p != nullptr && aligned(p, (size_t)size) && ld >= cols && ld <= kMaxPitch;
 }
 
+// A vector argument with n elements.
+bool vector_ok(const void* p, int64_t n, int64_t size) { return n == 0 || (p != nullptr && aligned(p, (size_t)size)); }
+
 msign_status_t check_block_operands(const ffn_block_t& b) {
   const int64_t s = dt_size(b.dtype);
   if (!matrix_ok(b.x, b.tokens, b.dim, b.ldx, s) || !matrix_ok(b.w_gate, b.hidden, b.dim, b.ld_gate, s) ||
@@ -580,7 +583,7 @@ msign_status_t add_rms_norm(const void* x, int64_t ldx, const void* residual, in
   if (tokens == 0 || dim == 0) return MSIGN_OK;
   const int64_t s = dt_size(dtype);
   if (!matrix_ok(x, tokens, dim, ldx, s) || !matrix_ok(y, tokens, dim, dim, s) ||
-      !matrix_ok(weight, 1, dim, dim, dt_size(w_dtype)) || !matrix_ok(rstd, 1, tokens, tokens, 4) ||
+      !vector_ok(weight, dim, dt_size(w_dtype)) || !vector_ok(rstd, tokens, 4) ||
       (residual != nullptr && (!matrix_ok(residual, tokens, dim, ldr, s) || !matrix_ok(h_out, tokens, dim, dim, s))))
     return fail(MSIGN_ERR_ARG, "tensors must be non-null, aligned to their elements, with pitches of at least a row "
                                "and at most 2^21 elements");
@@ -620,8 +623,8 @@ msign_status_t add_rms_norm_backward(const void* dy, int64_t ld_dy, const void* 
   if (dim == 0) return MSIGN_OK;
   const int64_t s = dt_size(dtype), w = dt_size(w_dtype);
   if (!matrix_ok(dy, tokens, dim, ld_dy, s) || !matrix_ok(h, tokens, dim, ldh, s) ||
-      !matrix_ok(rstd, 1, tokens, tokens, 4) || !matrix_ok(weight, 1, dim, dim, w) ||
-      !matrix_ok(dweight, 1, dim, dim, w) || !matrix_ok(dx, tokens, dim, dim, s) ||
+      !vector_ok(rstd, tokens, 4) || !vector_ok(weight, dim, w) ||
+      !vector_ok(dweight, dim, w) || !matrix_ok(dx, tokens, dim, dim, s) ||
       (dh != nullptr && !matrix_ok(dh, tokens, dim, ld_dh, s)))
     return fail(MSIGN_ERR_ARG, "tensors must be non-null, aligned to their elements, with pitches of at least a row "
                                "and at most 2^21 elements");
@@ -725,7 +728,7 @@ msign_status_t distill_topk(const void* logits, int64_t ld_logits, const void* i
   if (rows == 0) return MSIGN_OK;
   const int64_t s = dt_size(dtype), is = indices_64 ? 8 : 4, ts = dt_size(teacher_dtype);
   if (!matrix_ok(logits, rows, vocab, ld_logits, s) || !matrix_ok(indices, rows, top, top, is) ||
-      !matrix_ok(teacher, rows, top, top, ts) || !matrix_ok(loss, 1, rows, rows, 4) ||
+      !matrix_ok(teacher, rows, top, top, ts) || !vector_ok(loss, rows, 4) ||
       (dlogits != nullptr && (!matrix_ok(dlogits, rows, vocab, vocab, s) || grad == nullptr || !aligned(grad, 4))))
     return fail(MSIGN_ERR_ARG, "tensors must be non-null, aligned to their elements, with a pitch of at least a row "
                                "and at most 2^21 elements; dlogits needs grad");

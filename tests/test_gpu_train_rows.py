@@ -90,3 +90,32 @@ def test_norm_forward_in_place(kind, rows, dim):
     got = run(a, a, a)
     torch.cuda.synchronize()
     assert all(torch.equal(p, q) for p, q in zip(got, want))
+
+
+def test_more_rows_than_a_pitch_may_have_elements():
+    """Per-head norms and token-wise losses of short rows reach row counts past
+    2^21.  Compared on the GPU in 64 bits."""
+    M = require_gpu()
+    rows, dim = (1 << 21) + 5, 24
+    announce(f"norm {rows} x {dim}")
+    x, r, dy = (normal((rows, dim), 1.0, "bf16", 11 + i) for i in range(3))
+    w = normal((dim,), 0.2, "bf16", 14) + 1
+    y, h, rstd = M.add_rms_norm(x, w, r)
+    ry, rh, rs = R.rms(x.double(), r.double(), w.double(), 1e-6)
+    for got, want, tol in ((y, ry, row_tol("bf16")), (h, rh, row_tol("bf16")), (rstd, rs, 40 * U["f32"])):
+        assert float((got.double() - want).norm() / want.norm()) <= tol
+        assert float((got.double() - want).abs().max()) <= 60 * tol * float(want.square().mean().sqrt())
+    announce(f"norm backward {rows} x {dim}")
+    dx, dw = M.add_rms_norm_backward(dy, h, rstd, w)
+    rx, rw = R.rms_backward(dy.double(), h.double(), rstd.double(), w.double(), None)
+    assert float((dx.double() - rx).norm() / rx.norm()) <= row_tol("bf16")
+    assert float((dw.double() - rw).norm() / rw.norm()) <= row_tol("bf16")
+    del y, ry, rh, dx, rx
+    announce(f"distillation {rows} x {dim}")
+    idx = (torch.arange(rows, device="cuda") * 7 % dim)[:, None]
+    teacher = torch.zeros((rows, 1), device="cuda")
+    loss, dz = M.distill_topk_grad(x, idx, teacher, torch.tensor(1.0, device="cuda"))
+    logq = x.double().log_softmax(1)
+    assert float((loss.double() + logq.gather(1, idx)[:, 0]).abs().max()) <= 40 * U["f32"] * 12
+    want = logq.exp().scatter_add_(1, idx, torch.full_like(idx, -1, dtype=torch.float64))
+    assert float((dz.double() - want).norm() / want.norm()) <= row_tol("bf16")

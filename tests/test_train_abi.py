@@ -191,3 +191,19 @@ def test_binding_refuses_what_it_can_see():
         M.distill_topk_grad(x, idx, torch.zeros(4, 2), torch.zeros(3))
     with pytest.raises(ValueError, match="out"):
         M.distill_topk_grad(x, idx, torch.zeros(4, 2), torch.zeros(4), out=torch.zeros(4, 9))
+
+
+MOST_ROWS = 1 << 24
+
+
+@pytest.mark.parametrize("rows", [(1 << 21) + 1, MOST_ROWS])
+def test_row_operators_take_up_to_2_24_rows(rows):
+    """The vectors with one element a row have no pitch to refuse: a later
+    check answers."""
+    lib = _lib()
+    assert norm(lib, tokens=rows, y=at(0)) == ALIAS
+    assert norm_back(lib, tokens=rows, ws=None) == WORKSPACE
+    assert distill(lib, rows=rows, loss=at(0)) == ALIAS
+    assert norm(lib, tokens=MOST_ROWS + 1) == SHAPE and distill(lib, rows=MOST_ROWS + 1) == SHAPE
+    assert norm(lib, tokens=rows, rstd=None) == ARG and norm(lib, tokens=rows, rstd=at(5) + 2) == ARG
+    assert norm_back(lib, tokens=rows, rstd=None) == ARG and distill(lib, rows=rows, loss=at(4) + 2) == ARG
