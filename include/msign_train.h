@@ -13,7 +13,8 @@
  * every sum has a fixed order and no atomics are used.
  *
  * Matrices are row-major with unit stride along a row; a pitch is the
- * distance of two rows in elements, at least the row's length.  dtype is one
+ * distance of two rows in elements, at least the row's length and, where
+ * nothing else is said, at most 2^36.  dtype is one
  * of msign_dtype_t.  No output may overlap an input, another output or the
  * workspace, except where stated.
  */
@@ -36,7 +37,8 @@ typedef enum {
  *     g = x Wg^T,  u = x Wu^T,  h = a(g) * u,  y = h Wd^T
  * x [tokens, dim], w_gate and w_up [hidden, dim], w_down [dim, hidden], all
  * of `dtype`; ld_* are their pitches.  dim and hidden are at most 2^20,
- * tokens at most 2^24, pitches at most 2^21.
+ * tokens at most 2^24, pitches (those of the calls' other matrices too) at
+ * most 2^21.
  */
 typedef struct {
   int64_t tokens, dim, hidden;

@@ -28,6 +28,9 @@ msign_status_t hip_fail(hipError_t e, const char* what) {
 
 constexpr int64_t kMaxDim = int64_t(1) << 20, kMaxTokens = int64_t(1) << 24, kMaxPitch = int64_t(1) << 21;
 constexpr int64_t kMaxNormDim = 32768;
+// The products' offsets inside a tile have 32 bits, so kMaxPitch; the row
+// operators' have 64: here the bytes of kMaxTokens rows still do not overflow.
+constexpr int64_t kMaxRowPitch = int64_t(1) << 36;
 constexpr size_t kInvalid = (size_t)-1;
 
 bool dt_valid(int32_t dt) { return dt == MSIGN_F32 || dt == MSIGN_BF16 || dt == MSIGN_F16; }
@@ -230,9 +233,14 @@ msign_status_t check_block(const ffn_block_t* b) {
 }
 
 // A matrix argument: given, aligned to its elements, with a possible pitch.
-bool matrix_ok(const void* p, int64_t rows, int64_t cols, int64_t ld, int64_t size) {
+bool matrix_ok(const void* p, int64_t rows, int64_t cols, int64_t ld, int64_t size, int64_t most = kMaxPitch) {
   if (rows == 0 || cols == 0) return true;
-  return p != nullptr && aligned(p, (size_t)size) && ld >= cols && ld <= kMaxPitch;
+  return p != nullptr && aligned(p, (size_t)size) && ld >= cols && ld <= most;
+}
+
+// The same for the operators that take one row at a time.
+bool rows_ok(const void* p, int64_t rows, int64_t cols, int64_t ld, int64_t size) {
+  return matrix_ok(p, rows, cols, ld, size, kMaxRowPitch);
 }
 
 // A vector argument with n elements.
@@ -582,11 +590,11 @@ msign_status_t add_rms_norm(const void* x, int64_t ldx, const void* residual, in
   if (!(eps > 0.f) || !std::isfinite(eps)) return fail(MSIGN_ERR_ARG, "eps must be positive and finite");
   if (tokens == 0 || dim == 0) return MSIGN_OK;
   const int64_t s = dt_size(dtype);
-  if (!matrix_ok(x, tokens, dim, ldx, s) || !matrix_ok(y, tokens, dim, dim, s) ||
+  if (!rows_ok(x, tokens, dim, ldx, s) || !rows_ok(y, tokens, dim, dim, s) ||
       !vector_ok(weight, dim, dt_size(w_dtype)) || !vector_ok(rstd, tokens, 4) ||
-      (residual != nullptr && (!matrix_ok(residual, tokens, dim, ldr, s) || !matrix_ok(h_out, tokens, dim, dim, s))))
+      (residual != nullptr && (!rows_ok(residual, tokens, dim, ldr, s) || !rows_ok(h_out, tokens, dim, dim, s))))
     return fail(MSIGN_ERR_ARG, "tensors must be non-null, aligned to their elements, with pitches of at least a row "
-                               "and at most 2^21 elements");
+                               "and at most 2^36 elements");
   const Range hr = residual != nullptr ? range(h_out, tokens, dim, dim, s) : Range{nullptr, 0};
   const Range xr = range(x, tokens, dim, ldx, s), rr = range(residual, tokens, dim, ldr, s);
   const Range wr = range(weight, 1, dim, dim, dt_size(w_dtype));
@@ -622,12 +630,12 @@ msign_status_t add_rms_norm_backward(const void* dy, int64_t ld_dy, const void* 
   if (st != MSIGN_OK) return st;
   if (dim == 0) return MSIGN_OK;
   const int64_t s = dt_size(dtype), w = dt_size(w_dtype);
-  if (!matrix_ok(dy, tokens, dim, ld_dy, s) || !matrix_ok(h, tokens, dim, ldh, s) ||
+  if (!rows_ok(dy, tokens, dim, ld_dy, s) || !rows_ok(h, tokens, dim, ldh, s) ||
       !vector_ok(rstd, tokens, 4) || !vector_ok(weight, dim, w) ||
-      !vector_ok(dweight, dim, w) || !matrix_ok(dx, tokens, dim, dim, s) ||
-      (dh != nullptr && !matrix_ok(dh, tokens, dim, ld_dh, s)))
+      !vector_ok(dweight, dim, w) || !rows_ok(dx, tokens, dim, dim, s) ||
+      (dh != nullptr && !rows_ok(dh, tokens, dim, ld_dh, s)))
     return fail(MSIGN_ERR_ARG, "tensors must be non-null, aligned to their elements, with pitches of at least a row "
-                               "and at most 2^21 elements");
+                               "and at most 2^36 elements");
   const size_t need = add_rms_norm_backward_workspace_bytes(tokens, dim);
   if ((st = check_workspace(workspace, workspace_bytes, need)) != MSIGN_OK) return st;
   const Range dyr = range(dy, tokens, dim, ld_dy, s), dhr = range(dh, tokens, dim, ld_dh, s);
@@ -724,14 +732,14 @@ msign_status_t distill_topk(const void* logits, int64_t ld_logits, const void* i
     return fail(MSIGN_ERR_SHAPE, "rows must be in 0..2^24, vocab in 1..2^21 and top in 0..1024");
   if (!(tau > 0.f) || !std::isfinite(tau)) return fail(MSIGN_ERR_ARG, "tau must be positive and finite");
   if (indices_64 != 0 && indices_64 != 1) return fail(MSIGN_ERR_ARG, "indices_64 must be 0 or 1");
-  if (grad_stride < 0) return fail(MSIGN_ERR_ARG, "grad_stride must be >= 0");
+  if (grad_stride < 0 || grad_stride > kMaxRowPitch) return fail(MSIGN_ERR_ARG, "grad_stride must be in 0..2^36");
   if (rows == 0) return MSIGN_OK;
   const int64_t s = dt_size(dtype), is = indices_64 ? 8 : 4, ts = dt_size(teacher_dtype);
-  if (!matrix_ok(logits, rows, vocab, ld_logits, s) || !matrix_ok(indices, rows, top, top, is) ||
-      !matrix_ok(teacher, rows, top, top, ts) || !vector_ok(loss, rows, 4) ||
-      (dlogits != nullptr && (!matrix_ok(dlogits, rows, vocab, vocab, s) || grad == nullptr || !aligned(grad, 4))))
+  if (!rows_ok(logits, rows, vocab, ld_logits, s) || !rows_ok(indices, rows, top, top, is) ||
+      !rows_ok(teacher, rows, top, top, ts) || !vector_ok(loss, rows, 4) ||
+      (dlogits != nullptr && (!rows_ok(dlogits, rows, vocab, vocab, s) || grad == nullptr || !aligned(grad, 4))))
     return fail(MSIGN_ERR_ARG, "tensors must be non-null, aligned to their elements, with a pitch of at least a row "
-                               "and at most 2^21 elements; dlogits needs grad");
+                               "and at most 2^36 elements; dlogits needs grad");
   const Range zr = range(logits, rows, vocab, ld_logits, s), none = {nullptr, 0};
   const Range lossr = range(loss, 1, rows, rows, 4), dzr = range(dlogits, rows, vocab, vocab, s);
   const Range gr = dlogits != nullptr ? range(grad, rows, 1, grad_stride, 4) : none;

@@ -119,3 +119,31 @@ def test_more_rows_than_a_pitch_may_have_elements():
     assert float((loss.double() + logq.gather(1, idx)[:, 0]).abs().max()) <= 40 * U["f32"] * 12
     want = logq.exp().scatter_add_(1, idx, torch.full_like(idx, -1, dtype=torch.float64))
     assert float((dz.double() - want).norm() / want.norm()) <= row_tol("bf16")
+
+
+def test_row_operators_with_pitches_past_2_21():
+    """The last token's logits of each sequence and every n-th token's row."""
+    M = require_gpu()
+    announce("distillation of last tokens")
+    batch, length, vocab = 5, 41, 65539
+    logits = normal((batch, length, vocab), 2.0, "bf16", 21)
+    last = logits[:, -1]
+    assert last.stride(0) > 1 << 21
+    idx = torch.arange(batch * 3, device="cuda").view(batch, 3) * 4001
+    teacher = normal((batch, 3), 1.0, "f32", 22)
+    grad = torch.ones(batch, device="cuda")
+    got = M.distill_topk_grad(last, idx, teacher, grad)
+    want = M.distill_topk_grad(last.contiguous(), idx, teacher, grad)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    assert torch.equal(M.distill_topk(last, idx, teacher), want[0])
+    announce("norm of every 8193rd token")
+    wide = normal((4 * 8193, 257), 1.0, "bf16", 23)
+    x, r = wide[::8193], wide[1::8193]
+    assert x.stride(0) > 1 << 21
+    w = normal((257,), 0.2, "bf16", 24) + 1
+    y, h, rstd = M.add_rms_norm(x, w, r)
+    want = M.add_rms_norm(x.contiguous(), w, r.contiguous())
+    assert all(torch.equal(a, b) for a, b in zip((y, h, rstd), want))
+    got = M.add_rms_norm_backward(r, x, rstd, w, dh=wide[2::8193])
+    want = M.add_rms_norm_backward(r.contiguous(), x.contiguous(), rstd, w, dh=wide[2::8193].contiguous())
+    assert all(torch.equal(a, b) for a, b in zip(got, want))

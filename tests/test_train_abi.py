@@ -207,3 +207,19 @@ def test_row_operators_take_up_to_2_24_rows(rows):
     assert norm(lib, tokens=MOST_ROWS + 1) == SHAPE and distill(lib, rows=MOST_ROWS + 1) == SHAPE
     assert norm(lib, tokens=rows, rstd=None) == ARG and norm(lib, tokens=rows, rstd=at(5) + 2) == ARG
     assert norm_back(lib, tokens=rows, rstd=None) == ARG and distill(lib, rows=rows, loss=at(4) + 2) == ARG
+
+
+def test_row_operators_take_any_pitch_that_memory_holds():
+    """The last token's logits of every sequence, or every thousandth row, have
+    pitches past the products' limit: a later check answers."""
+    lib = _lib()
+    far = 1 << 31
+    assert norm(lib, ldx=far, y=at(0)) == ALIAS and norm(lib, ldr=far, y=at(0)) == ALIAS
+    for pitch in ("ld_dy", "ldh", "ld_dh"):
+        assert norm_back(lib, ws=None, **{pitch: far}) == WORKSPACE
+    assert distill(lib, ldz=far, loss=at(0)) == ALIAS
+    # rows that reach into an output are still seen
+    assert norm(lib, ldx=far, y=at(0) + 4 * far) == ALIAS
+    too_far = (1 << 36) + 1
+    assert norm(lib, ldx=too_far) == ARG and norm_back(lib, ldh=too_far) == ARG and distill(lib, ldz=too_far) == ARG
+    assert distill(lib, stride=too_far) == ARG
