@@ -18,6 +18,7 @@ from ._binding import _STATUS, MsignError, _load
 _DT = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
 ACTIVATIONS = {"silu": 0, "gelu": 1}  # FFN_SILU, FFN_GELU
 MAX_TOP = 1024  # DISTILL_MAX_TOP
+_FAR = 1 << 21  # the products' largest pitch
 
 
 class _Block(ctypes.Structure):
@@ -85,17 +86,17 @@ def _like(t: torch.Tensor) -> torch.Tensor:
     return torch.empty_like(t) if t.is_contiguous() else torch.empty_like(t, memory_format=torch.contiguous_format)
 
 
-def _matrix(t: torch.Tensor):
+def _matrix(t: torch.Tensor, most: int = 1 << 36):
     """t as [rows, last dim] with unit stride along a row and rows that do
-    not overlap, a view where the strides allow it and else a copy:
-    (tensor, address, rows, cols, pitch)."""
+    not overlap, at most `most` elements apart, a view where the strides allow
+    it and else a copy: (tensor, address, rows, cols, pitch)."""
     cols = t.shape[-1]
     if t.is_contiguous():
         rows = t.shape[0] if t.dim() == 2 else _prod(t.shape[:-1])
         return t, t.data_ptr(), rows, cols, cols or 1
     if t.dim() != 2:
         t = t.reshape(-1, cols)
-    if (cols > 1 and t.stride(1) != 1) or (t.shape[0] > 1 and t.stride(0) < cols):
+    if (cols > 1 and t.stride(1) != 1) or (t.shape[0] > 1 and not cols <= t.stride(0) <= most):
         t = t.contiguous()
     rows = t.shape[0]
     return t, t.data_ptr(), rows, cols, t.stride(0) if rows > 1 else cols
@@ -153,10 +154,10 @@ def _block(x, w_gate, w_up, w_down, activation):
     if w_gate.dtype != dtype or w_up.dtype != dtype or w_down.dtype != dtype:
         raise ValueError("x and the weights must share one dtype")
     device = _same_device(x, w_gate, w_up, w_down)
-    x, px, tokens, _, ldx = _matrix(x)
-    w_gate, pg, _, _, ldg = _matrix(w_gate)
-    w_up, pu, _, _, ldu = _matrix(w_up)
-    w_down, pd, _, _, ldd = _matrix(w_down)
+    x, px, tokens, _, ldx = _matrix(x, _FAR)
+    w_gate, pg, _, _, ldg = _matrix(w_gate, _FAR)
+    w_up, pu, _, _, ldu = _matrix(w_up, _FAR)
+    w_down, pd, _, _, ldd = _matrix(w_down, _FAR)
     b = _Block(tokens, dim, hidden, _dtype(x), act, px, pg, pu, pd, ldx, ldg, ldu, ldd)
     return b, device, (x, w_gate, w_up, w_down)
 
@@ -197,9 +198,9 @@ def gated_ffn_backward(dy: torch.Tensor, x: torch.Tensor, w_gate: torch.Tensor, 
     if dy.dtype != x.dtype or g.dtype != x.dtype or u.dtype != x.dtype:
         raise ValueError("dy, g and u must have x's dtype")
     _same_device(x, dy, g, u)
-    dy, pdy, _, _, ld_dy = _matrix(dy)
-    g, pg, _, _, ld_act = _matrix(g)
-    u, pu, _, _, ld_u = _matrix(u)
+    dy, pdy, _, _, ld_dy = _matrix(dy, _FAR)
+    g, pg, _, _, ld_act = _matrix(g, _FAR)
+    u, pu, _, _, ld_u = _matrix(u, _FAR)
     if ld_act != ld_u:
         g, pg, _, _, ld_act = _matrix(g.contiguous())
         u, pu, _, _, ld_u = _matrix(u.contiguous())
