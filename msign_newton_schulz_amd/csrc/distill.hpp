@@ -24,6 +24,8 @@
 #include "gemm_nt.hpp"
 #include "row_ops.hpp"
 
+#include <cfloat>
+
 namespace msign {
 namespace distill {
 
@@ -146,7 +148,8 @@ __global__ void __launch_bounds__(NT, OCC) row_kernel(const Args a) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int n = a.vocab;
   const int whole = n / CE, tail = n % CE;  // chunks and single elements
-  const float k = 1.44269504f / a.tau;
+  // (finite at any tau: the largest logit's difference is 0 and stays 0)
+  const float k = fminf(1.44269504f / a.tau, FLT_MAX);
   auto zrow = [&](int64_t row) { return static_cast<const char*>(a.z) + row * a.ldz * Elem<T>::size; };
 
   constexpr int KEEP = C > 0 ? C : 1;

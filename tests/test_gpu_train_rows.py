@@ -147,3 +147,33 @@ def test_row_operators_with_pitches_past_2_21():
     got = M.add_rms_norm_backward(r, x, rstd, w, dh=wide[2::8193])
     want = M.add_rms_norm_backward(r.contiguous(), x.contiguous(), rstd, w, dh=wide[2::8193].contiguous())
     assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("tau", [1e-42, 1e-39, 1e-37, 1e-20])
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+def test_distill_at_tiny_temperatures(kind, tau):
+    """Below 2^-128 log2(e) the reciprocal of tau is past fp32's range; the
+    softmax is then one at the largest logit.  With p and q there, loss =
+    tau sum_k p_k (t_k - t_max - z_k + z_max) up to tau^2 log terms, and the
+    gradient is tau grad (q - p), both exact up to fp32's rounding and, for
+    the smallest, its last place 2^-149."""
+    M = require_gpu()
+    announce(f"distill tau {tau} {kind}")
+    for vocab in (50, 5000, 170001):
+        z = normal((3, vocab), 2.0, kind, 31)
+        idx = torch.tensor([[1, 7, 20], [3, 4, 5], [0, 30, 49]], device="cuda")
+        teacher = torch.tensor([[2.0, 1.0, 0.0], [0.0, 3.0, 1.0], [1.0, 0.0, 2.0]], device="cuda")
+        z[0, 1] = 40.0  # the student agrees
+        z[1, 9] = 40.0  # it does not
+        z[2, 49] = 40.0
+        grad = torch.tensor([1.0, 1.0, 0.5], device="cuda")
+        loss, dz = M.distill_topk_grad(z, idx, teacher, grad, temperature=tau)
+        only = M.distill_topk(z, idx, teacher, temperature=tau)
+        want = tau * torch.tensor([0.0, 40.0 - float(z[1, 4]), 0.0], dtype=torch.float64, device="cuda")
+        slack = 1e-5 * tau + 2.0 ** -149
+        assert float((loss.double() - want).abs().max()) <= 100 * slack
+        assert torch.equal(loss, only)
+        full = torch.zeros((3, vocab), dtype=torch.float64, device="cuda")
+        full[1, 9], full[1, 4] = tau, -tau
+        # (bf16 holds the gradient itself to 2^-8, and to 2^-133 below its normal range)
+        assert float((dz.double() - full).abs().max()) <= (2.0 ** -8 * tau + 2.0 ** -133 if kind == "bf16" else slack)
