@@ -150,8 +150,10 @@ ffn::Plan plan_product(int64_t m, int64_t n, int64_t count, int64_t k, int64_t s
 
 struct ForwardPlan {
   Operand x, wg, wu, wd;
-  size_t h, partial, total;
+  size_t h, total;
   int64_t ldh;
+  bool few;  // the kernels for a few tokens; else:
+  size_t partial;
   ffn::Plan gated, down;
 };
 
@@ -173,7 +175,7 @@ bool skinny(const ffn_block_t& b) {
 
 ForwardPlan plan_forward(const ffn_block_t& b) {
   const int64_t size = dt_size(b.dtype);
-  ForwardPlan p;
+  ForwardPlan p = {};
   Carver c;
   p.x = operand(b.x, b.ldx, b.tokens, b.dim, size, c);
   p.wg = operand(b.w_gate, b.ld_gate, b.hidden, b.dim, size, c);
@@ -181,10 +183,13 @@ ForwardPlan plan_forward(const ffn_block_t& b) {
   p.wd = operand(b.w_down, b.ld_down, b.dim, b.hidden, size, c);
   p.ldh = round_up(b.hidden, 64);
   p.h = c.take(b.tokens * p.ldh * size);
-  p.gated = plan_product(b.tokens, 2 * b.hidden, 1, b.dim, 1, b.dtype, true);
-  p.down = plan_product(b.tokens, b.dim, 1, b.hidden, 1, b.dtype, true);
-  p.partial = c.take((int64_t)(p.gated.partial_bytes > p.down.partial_bytes ? p.gated.partial_bytes
-                                                                            : p.down.partial_bytes));
+  p.few = skinny(b);
+  if (!p.few) {
+    p.gated = plan_product(b.tokens, 2 * b.hidden, 1, b.dim, 1, b.dtype, true);
+    p.down = plan_product(b.tokens, b.dim, 1, b.hidden, 1, b.dtype, true);
+    p.partial = c.take((int64_t)(p.gated.partial_bytes > p.down.partial_bytes ? p.gated.partial_bytes
+                                                                              : p.down.partial_bytes));
+  }
   p.total = c.off;
   return p;
 }
@@ -378,7 +383,7 @@ msign_status_t ffn_forward(const ffn_block_t* bp, void* y, int64_t ldy, void* ga
       (e = resolve(p.wu, s, ws, stream, &wu)) != hipSuccess || (e = resolve(p.wd, s, ws, stream, &wd)) != hipSuccess)
     return hip_fail(e, "pad_copy_kernel");
 
-  if (skinny(b)) {
+  if (p.few) {
     const int64_t ce = 16 / s;
     ffn::SkinnyArgs k;
     std::memset(&k, 0, sizeof(k));

@@ -223,3 +223,11 @@ def test_row_operators_take_any_pitch_that_memory_holds():
     too_far = (1 << 36) + 1
     assert norm(lib, ldx=too_far) == ARG and norm_back(lib, ldh=too_far) == ARG and distill(lib, ldz=too_far) == ARG
     assert distill(lib, stride=too_far) == ARG
+
+
+@pytest.mark.parametrize("dtype,size", [(0, 4), (1, 2), (2, 2)])
+@pytest.mark.parametrize("tokens,dim,hidden", [(1, 1024, 4096), (16, 4096, 4096), (32, 512, 2048)])
+def test_ffn_workspace_of_a_few_tokens_is_the_hidden_activations(tokens, dim, hidden, dtype, size):
+    """The kernels for a few tokens split no tiles, so need no room for parts."""
+    need = _lib().ffn_forward_workspace_bytes(block(tokens=tokens, dim=dim, hidden=hidden, dtype=dtype))
+    assert need == tokens * hidden * size
