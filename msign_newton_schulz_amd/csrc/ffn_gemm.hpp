@@ -145,7 +145,7 @@ struct Tile {
 template <int OFF>
 __device__ __forceinline__ void load_lds(const u32x4& rsrc, int off, uint32_t base) {
   asm volatile("s_add_u32 m0, %0, %3\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
-               :: "s"(base), "v"(off), "s"(rsrc), "n"(OFF * 16) : "memory", "scc");
+               :: "s"(base), "v"(off), "s"(rsrc), "n"(OFF * 16) : "memory", "m0", "scc");
 }
 
 __device__ __forceinline__ u32x4 make_rsrc(const char* base, int bytes) {

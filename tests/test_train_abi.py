@@ -231,3 +231,18 @@ def test_ffn_workspace_of_a_few_tokens_is_the_hidden_activations(tokens, dim, hi
     """The kernels for a few tokens split no tiles, so need no room for parts."""
     need = _lib().ffn_forward_workspace_bytes(block(tokens=tokens, dim=dim, hidden=hidden, dtype=dtype))
     assert need == tokens * hidden * size
+
+
+def test_assembly_declares_the_registers_that_it_names():
+    """m0 and the condition registers are the compiler's too: a statement that
+    writes one lists it."""
+    folder = os.path.join(ROOT, "msign_newton_schulz_amd", "csrc")
+    seen = 0
+    for name in sorted(os.listdir(folder)):
+        for stmt in re.findall(r"\basm\b[^;]*;", open(os.path.join(folder, name)).read()):
+            code, _, lists = stmt.partition("::") if "::" in stmt else stmt.partition(" : ")
+            for reg in ("m0", "vcc", "exec"):
+                if re.search(rf"\b{reg}\b", code):
+                    seen += 1
+                    assert f'"{reg}"' in lists, (name, stmt)
+    assert seen > 0
