@@ -3,12 +3,14 @@
 Argument marshalling only, as in `_binding`: torch provides device memory and
 the stream, every step of the computation runs in the HIP library, and there
 is no fallback.  Outputs are queued on the current stream of the inputs'
-device.
+device.  Nothing here records an autograd graph: a gradient is a call of its
+own, and a forward call that an autograd graph leads into warns.
 """
 
 from __future__ import annotations
 
 import ctypes
+import warnings
 from typing import Optional, Tuple
 
 import torch
@@ -128,6 +130,18 @@ def _current_stream(index: int) -> int:
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _current_stream)
 
 
+def _no_graph(name: str, gradient: str, *tensors) -> None:
+    """Warns where autograd would expect a graph from `name`'s inputs to its
+    outputs."""
+    if not torch.is_grad_enabled():
+        return
+    for t in tensors:
+        if t is not None and t.requires_grad:
+            warnings.warn(f"{name} records no autograd graph, so no gradient reaches its inputs through its outputs: "
+                          f"call {gradient} for it, under torch.no_grad() or with detached tensors", stacklevel=3)
+            return
+
+
 def _scratch(nbytes: int, device, workspace: Optional[torch.Tensor]):
     """(pointer, bytes, owner) of a workspace of at least nbytes."""
     if nbytes == (1 << 64) - 1:
@@ -170,9 +184,10 @@ def gated_ffn(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, w_down:
     x [..., dim], w_gate and w_up [hidden, dim], w_down [dim, hidden], one
     dtype (float32, bfloat16 or float16).  Returns y [..., dim], or with
     `save` (y, g, u), where g and u [..., hidden] are what
-    `gated_ffn_backward` takes."""
+    `gated_ffn_backward` takes.  No autograd graph is recorded."""
     lib = _library()
     b, device, owners = _block(x, w_gate, w_up, w_down, activation)
+    _no_graph("gated_ffn", "gated_ffn_backward", x, w_gate, w_up, w_down)
     y = _like(x)
     g = u = None
     pg = pu = None
@@ -219,7 +234,8 @@ def add_rms_norm(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torch
 
     Returns (y, h, rstd): y and h in x's dtype (h is x itself without a
     residual), rstd float32 with x's shape without the last dimension.
-    weight [dim] may have another dtype than x."""
+    weight [dim] may have another dtype than x.  No autograd graph is
+    recorded: `add_rms_norm_backward` takes h and rstd."""
     lib = _library()
     shape = x.shape
     if x.dim() < 1 or weight.dim() != 1 or weight.shape[0] != shape[-1]:
@@ -227,6 +243,7 @@ def add_rms_norm(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torch
     if residual is not None and (residual.shape != shape or residual.dtype != x.dtype):
         raise ValueError("residual must have x's shape and dtype")
     device = _same_device(x, weight, residual)
+    _no_graph("add_rms_norm", "add_rms_norm_backward", x, weight, residual)
     w = weight.contiguous()
     x2, px, rows, dim, ldx = _matrix(x)
     y = _like(x)
@@ -299,7 +316,9 @@ def distill_topk(logits: torch.Tensor, indices: torch.Tensor, teacher: torch.Ten
 
     indices [..., top] (int32 or int64; entries outside 0 .. vocab - 1, such
     as -1, are padding) and teacher [..., top] of any float dtype.  Returns
-    float32 [...]; a row with padding only has loss 0."""
+    float32 [...]; a row with padding only has loss 0.  No autograd graph is
+    recorded: `distill_topk_grad` gives the logits' gradient."""
+    _no_graph("distill_topk", "distill_topk_grad", logits, teacher)
     return _distill(logits, indices, teacher, temperature, None, None)
 
 
