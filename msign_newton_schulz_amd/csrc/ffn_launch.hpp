@@ -94,12 +94,23 @@ hipError_t launch_typed(Kind kind, const Plan& plan, const Args<kMaxProblems>& a
   }
 }
 
-// In one launch where both take the same number of workgroups a CU.  Else a CU
-// would hold one workgroup where it can hold two of the smaller kind: in one
-// launch if all the blocks are two rounds or less, for the gaps saved, else one
-// after the other (bf16, us of the backward pass in one and in two: 200 tokens of
-// 1500 x 2000 39 and 47, of 136 x 700 25 and 27; 900 of 1500 x 3300 95 and 92, 64
-// of 4096 x 14336 261 and 207).
+// In one launch where both take the same number of workgroups a CU: at few
+// rounds one's blocks fill the CUs that the other's last round leaves, at many
+// rounds it makes no difference.  (bf16, us of the backward pass in one launch
+// and in two, by rounds of their blocks: one, 400 tokens of 1000 x 1000 32 and 35;
+// two, 1000 of 600 x 700 42 and 49, 1024 of 1024 x 4096 79 and 85, 4096 of them
+// 222 and 230, 16384 of them 797 and 789; four, 4096 of 2048 x 7168 642 and 641;
+// twelve, 4096 of 4096 x 14336 2261 and 2262; thirteen, 8192 of them 4457 and
+// 4465.)
+// Of tiles of two kinds a CU would hold one workgroup where it can hold two of
+// the smaller kind: in one launch if all the blocks are two rounds or less, for
+// the gaps saved, else one after the other.  (X 8 for dx in 128-tiles of 8 chunks
+// and so on.  Two rounds or less: X 8 and W 16, 2767 tokens of 16 x 477 47 and 53;
+// X 16 and W 8, 13 of 700 x 900 36 and 40; X 8 and W 256, 417 of 9335 x 338 82 and
+// 90; X 256 and W 8, 2192 of 4531 x 376 115 and 126.  More: X 8 and W 16, 8625 of
+// 8174 x 18 337 and 334; X 16 and W 8, 64 of 4096 x 14336 281 and 228; X 8 and W
+// 256, 900 of 1500 x 3300 130 and 130; X 256 and W 8, 2942 of 380 x 11706 325 and
+// 298.)
 template <typename T>
 hipError_t launch_dx_dw_typed(const Plan& px, const Plan& pw, const Args<kMaxProblems>& dx,
                               const Args<kMaxProblems>& dw, hipStream_t st) {
@@ -123,8 +134,9 @@ hipError_t launch_dx_dw_typed(const Plan& px, const Plan& pw, const Args<kMaxPro
       return pw.rows == 256 ? launch_pair<X16, W256>(px, pw, dx, dw, st) : launch_pair<X16, W16>(px, pw, dx, dw, st);
     }
     if (px.blocks + pw.blocks <= 512) {
-      if (two_x && pw.rows == 256) return launch_pair<X8, W256>(px, pw, dx, dw, st);
-      if (two_w && px.rows == 128) return launch_pair<X16, W8>(px, pw, dx, dw, st);
+      if (two_x)
+        return pw.rows == 256 ? launch_pair<X8, W256>(px, pw, dx, dw, st) : launch_pair<X8, W16>(px, pw, dx, dw, st);
+      return px.rows == 256 ? launch_pair<X256, W8>(px, pw, dx, dw, st) : launch_pair<X16, W8>(px, pw, dx, dw, st);
     }
     const hipError_t e = two_x             ? launch_tile<X8>(px, dx, 1, st)
                          : px.rows == 256 ? launch_tile<X256>(px, dx, 1, st)
