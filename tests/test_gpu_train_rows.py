@@ -177,3 +177,85 @@ def test_distill_at_tiny_temperatures(kind, tau):
         full[1, 9], full[1, 4] = tau, -tau
         # (bf16 holds the gradient itself to 2^-8, and to 2^-133 below its normal range)
         assert float((dz.double() - full).abs().max()) <= (2.0 ** -8 * tau + 2.0 ** -133 if kind == "bf16" else slack)
+
+
+def close(got, want, tol):
+    """Relative in the 2-norm and, for every element, in multiples of the mean
+    size."""
+    d = (got.double() - want).abs()
+    assert float(d.norm()) <= tol * float(want.norm())
+    assert float(d.max()) <= 60 * tol * float(want.square().mean().sqrt())
+
+
+# More rows than resident workgroups (4096 of 64 threads, 768 or 1024 of 256,
+# 512 of 512, 256 of 1024), in every configuration of the forward pass.
+@pytest.mark.parametrize("kind,rows,dim", [("bf16", 5000, 96), ("f16", 4500, 1000), ("bf16", 1500, 2003),
+                                           ("bf16", 900, 4099), ("f16", 600, 8200), ("bf16", 300, 12001),
+                                           ("bf16", 300, 30001), ("f32", 5000, 95), ("f32", 900, 2051),
+                                           ("f32", 300, 20001)])
+@pytest.mark.parametrize("with_residual", [True, False])
+def test_norm_walks_over_rows(kind, rows, dim, with_residual):
+    """Every row, compared on the GPU in 64 bits."""
+    M = require_gpu()
+    announce(f"norm walk {rows} {dim} {kind} {with_residual}")
+    x = normal((rows, dim), 1.0, kind, 41)
+    x *= (1 + torch.arange(rows, device="cuda") % 7)[:, None].to(x.dtype)  # (neighbouring rows have other norms)
+    r = normal((rows, dim), 1.0, kind, 42) if with_residual else None
+    w = normal((dim,), 0.2, kind, 43) + 1
+    y, h, rstd = M.add_rms_norm(x, w, r)
+    ry, rh, rs = R.rms(x.double(), None if r is None else r.double(), w.double(), 1e-6)
+    close(y, ry, row_tol(kind))
+    close(rstd, rs, 40 * U["f32"])
+    if with_residual:
+        close(h, rh, row_tol(kind))
+
+
+def test_norm_backward_walks_over_rows_of_one_wave():
+    """Four rows a workgroup and more of them than 768 workgroups take at once."""
+    M = require_gpu()
+    for kind, rows, dim in (("bf16", 4001, 96), ("f32", 7003, 251), ("f16", 3500, 1000)):
+        announce(f"norm backward walk {rows} {dim} {kind}")
+        dy, h, dh = (normal((rows, dim), 1.0, kind, 51 + i) for i in range(3))
+        w = normal((dim,), 0.2, kind, 55) + 1
+        rstd = (h.double().square().mean(1) + 1e-6).rsqrt().float()
+        dx, dw = M.add_rms_norm_backward(dy, h, rstd, w, dh=dh)
+        rx, rw = R.rms_backward(dy.double(), h.double(), rstd.double(), w.double(), dh.double())
+        close(dx, rx, row_tol(kind))
+        # (f32: sums over the rows, as a product's)
+        close(dw, rw, 100 * U["f32"] if kind == "f32" else row_tol(kind))
+
+
+# Resident workgroups: 3072 of 64 threads, 1792 (loss), 1280, 1024 or 768 of
+# 256, 512 or 256 of 512, 256 of 1024.
+@pytest.mark.parametrize("kind,rows,vocab", [("bf16", 1500, 5), ("bf16", 4000, 130), ("f16", 3500, 3001), ("bf16", 1500, 6001),
+                                             ("bf16", 1500, 12001), ("f16", 900, 30001), ("bf16", 600, 60001),
+                                             ("bf16", 300, 90001), ("bf16", 300, 170003), ("bf16", 300, 40001),
+                                             ("f32", 4000, 70), ("f32", 1500, 3003), ("f32", 900, 15001),
+                                             ("f32", 300, 85001)])
+def test_distill_walks_over_rows(kind, rows, vocab):
+    """Loss alone and with the gradient, every row, compared on the GPU in 64
+    bits."""
+    M = require_gpu()
+    announce(f"distill walk {rows} {vocab} {kind}")
+    tau, top = 1.5, 4
+    z = normal((rows, vocab), 1.0, kind, 61)
+    z *= (1 + torch.arange(rows, device="cuda") % 3)[:, None].to(z.dtype)
+    g = torch.Generator().manual_seed(62)
+    idx = torch.randint(0, vocab, (rows, top), generator=g).cuda()
+    teacher = normal((rows, top), 2.0, "f32", 63)
+    grad = (torch.rand(rows, generator=g) + 0.5).cuda()
+    loss, dz = M.distill_topk_grad(z, idx, teacher, grad, temperature=tau)
+    only = M.distill_topk(z, idx, teacher, temperature=tau)
+    logp, logq = (teacher.double() / tau).log_softmax(1), (z.double() / tau).log_softmax(1)
+    want = tau * tau * (logp.exp() * (logp - logq.gather(1, idx))).sum(1)
+    # (a difference of logarithms up to log(vocab) <= 12.1 and of scores)
+    size = tau * tau * (12.1 + float(z.abs().max()) / tau)
+    for got in (loss, only):
+        assert float((got.double() - want).abs().max()) <= 40 * U["f32"] * size
+    full = logq.exp_().scatter_add_(1, idx, -logp.exp()).mul_((tau * grad.double())[:, None])
+    # (f16 gradients fall below its normal range: their rounding is absolute there)
+    close_norm = row_tol(kind) * float(full.norm()) + (2.0 ** -25 * full.numel() ** 0.5 if kind == "f16"
+                                                       else 40 * U["f32"] * tau * float(grad.norm()))
+    assert float((dz.double() - full).norm()) <= close_norm
+    per_row = (dz.double() - full).norm(dim=1) - 3 * row_tol(kind) * full.norm(dim=1)
+    assert float(per_row.max()) <= (2.0 ** -25 * vocab ** 0.5 if kind == "f16" else 40 * U["f32"] * tau * 1.5)
