@@ -16,7 +16,8 @@
  * distance of two rows in elements, at least the row's length and, where
  * nothing else is said, at most 2^36.  dtype is one
  * of msign_dtype_t.  No output may overlap an input, another output or the
- * workspace, except where stated.
+ * workspace, except where stated; a matrix counts from its first to its last
+ * element, with what lies between its rows.
  */
 #ifndef MSIGN_TRAIN_H_
 #define MSIGN_TRAIN_H_

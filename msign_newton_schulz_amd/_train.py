@@ -184,7 +184,9 @@ def gated_ffn(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, w_down:
     x [..., dim], w_gate and w_up [hidden, dim], w_down [dim, hidden], one
     dtype (float32, bfloat16 or float16).  Returns y [..., dim], or with
     `save` (y, g, u), where g and u [..., hidden] are what
-    `gated_ffn_backward` takes.  No autograd graph is recorded."""
+    `gated_ffn_backward` takes.  Sums are in float32; a(g) * u is rounded
+    once to the dtype for the second product (with float16, values past 65504
+    become infinite).  No autograd graph is recorded."""
     lib = _library()
     b, device, owners = _block(x, w_gate, w_up, w_down, activation)
     _no_graph("gated_ffn", "gated_ffn_backward", x, w_gate, w_up, w_down)
@@ -205,7 +207,9 @@ def gated_ffn_backward(dy: torch.Tensor, x: torch.Tensor, w_gate: torch.Tensor, 
                        workspace: Optional[torch.Tensor] = None
                        ) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor, torch.Tensor]:
     """Gradients of `gated_ffn` (C ABI `ffn_backward`) from dy, the gradient of
-    y, and the saved g and u: (dx, dw_gate, dw_up, dw_down)."""
+    y, and the saved g and u: (dx, dw_gate, dw_up, dw_down).  Sums are in
+    float32; a(g) * u and the gradients of g and u are rounded once to the
+    dtype for the products that take them."""
     lib = _library()
     b, device, owners = _block(x, w_gate, w_up, w_down, activation)
     if dy.shape != x.shape or g.shape != x.shape[:-1] + (b.hidden,) or u.shape != g.shape:

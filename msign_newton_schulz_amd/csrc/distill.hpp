@@ -18,7 +18,11 @@
 // for the first; loading the next row into the registers that this row's
 // gradient leaves, with no branch, so that loads are counted, made the rest.  The
 // loss alone: 256 MB of rows of 32768 47 us, 5.7 TB/s; 32 rows of 32000 6.9 us,
-// latency.
+// latency.  The teacher's entries are compared with one another for equal indices,
+// which long lists pay for (bf16, us with the gradient, 8 / 64 / 128 / 256 / 512 /
+// 1024 entries: 16384 x 8192 127 / 145 / 183 / 271 / 802 / 2911; 4194 x 32000 114 /
+// 131 / 147 / 182 / 419 / 1407; 1024 x 131072 124 / 128 / 142 / 169 / 237 / 549; the
+// loss alone 67 to 126, 51 to 92, 51 to 65).
 #pragma once
 
 #include "gemm_nt.hpp"

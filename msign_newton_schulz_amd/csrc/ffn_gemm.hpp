@@ -28,7 +28,8 @@
 // 1652 TFLOP/s both along K, 1267 to 1435 with B K-major, 905 to 921 with both):
 //   8192 tokens: gated 1435 us, 1341 TFLOP/s; down 665 us, 1447 TFLOP/s
 //   4096 tokens: dgated 458 us, 1050 TFLOP/s; dx and the three weight gradients
-//   in one launch 1766 us, 1362 TFLOP/s (apart 650 and 1092, 1480 and 1322)
+//   in one launch 1766 us, 1362 TFLOP/s (apart 650 and 1092; timed in turn, the
+//   whole pass takes the same either way, 2261 and 2262 us)
 //   16 tokens: gated 42 us, 5.6 TB/s; down 23 us, 5.1 TB/s, bound by memory
 // Bound by the matrix instructions at the clock that the power limit leaves
 // (down: busy 80 % of the time at 1.77 GHz, gated 72 % at 1.72 GHz).  dgated
@@ -576,7 +577,6 @@ __device__ __forceinline__ void tile_block(const Args<C::NG>& a, const Problem& 
   constexpr int NA = C::BM * C::CPR, NB = C::BN * C::CPR;  // chunks of a stage
   u32x4* const lds_a[2] = {lds, lds + NA};
   u32x4* const lds_b[2] = {lds + 2 * NA, lds + 2 * NA + NB};
-  const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   const int wm = wave / C::WGN, wn = wave % C::WGN;
 

@@ -8,7 +8,8 @@
 // split the sum over K; their sums meet in LDS in wave order.  Against tiles this
 // saves the passes that join parts and, in fp32, the 128 rows that a tile
 // multiplies.  Measured with both products (weights once): bf16, 1 token, 1024 x
-// 4096 5.4 and 7.1 us, latency; 4096 x 8192 38 us a call, 5.3 TB/s; fp32, 1
+// 4096 5.6 and 7.0 us, the second with 64 workgroups for 256 CUs; 4096 x 8192 38 us
+// a call, 5.3 TB/s; fp32, 1
 // token, 4096 x 14336 136 us, 5.2 TB/s, 16 tokens 180 us, where the tokens'
 // fragments take as much cache bandwidth as the weights.  Two groups of rows a
 // workgroup, to share them, took 165 us there and 44 us in the bf16 case, for

@@ -7,11 +7,13 @@
 // registers; the workgroups' sums are added by a second kernel in a fixed
 // order.  The next row is loaded before this one is reduced (HOLD; wide rows
 // leave no registers for that and read the weight again each time).  Bound by
-// memory.  Measured, bf16, 16384 x 4096: forward, two reads and two writes of
-// 134 MB, 97 us, 5.6 TB/s (a large copy 5.2); backward, three and one, 83 us with
-// dh and dy one tensor, 6.5 TB/s; 8192 x 4096 of four tensors 54 us, 4.9 TB/s. One
-// row of 4096: 2.9 us, a launch and two rounds of latency.  Without HOLD the
-// backward pass waits for each row's loads: 24000 columns of 16 bits 3.0 TB/s.
+// memory.  Measured, bf16, 16384 x 4096, four sets of tensors in turn: forward, two
+// reads and two writes of 134 MB, 98 us, 5.5 TB/s (a large copy 5.2); backward,
+// three and one, 108 us, 5.0 TB/s; rows off 16 bytes, f16, 5001 x 4099, 46 us, 3.6
+// TB/s, 5 of them the second kernel's.  One row of 4096: 2.9 us, a launch and two
+// rounds of latency.  Without HOLD the backward pass waits for each row's loads, and
+// reads dh and the weight between its stores: 24000 columns of 16 bits 86 us for
+// 268 MB, 3.1 TB/s.
 #pragma once
 
 #include "row_ops.hpp"

@@ -525,8 +525,8 @@ hipError_t norm_forward_cfg(const norm::ForwardArgs& a, hipStream_t st) {
 // (three waves per SIMD are the most that the registers allow; two with more than
 // two chunks a thread), one of 512.  With 1024 workgroups a part of the
 // rows waits for a second turn, and there are more partial sums of the weight's
-// gradient to write and add (bf16, 16384 x 4096: 84 and 96 us; 8192 x 8192 in 512
-// threads 92 and 99 us).
+// gradient to write and add (bf16, dh and dy one tensor: 16384 x 4096 84 and 96 us;
+// 8192 x 8192 in 512 threads 92 and 99 us).
 constexpr int64_t kNormBackwardBlocks = 256 * 3;
 
 template <typename T, int NT, int C, bool HOLD>
@@ -545,8 +545,9 @@ hipError_t norm_backward_cfg(const norm::BackwardArgs& a, int64_t& blocks, hipSt
 // in two workgroups a CU instead of one, or the next row held instead of the
 // weight read again (bf16, 268 MB in all, us here and in the forward pass's
 // configuration: dim 4104 57 and 77, 5120 54 and 66, 8192 55 and 57, 8200 66 and
-// 82, 16384 61 and 62, 24000 90 and 112).  In the forward pass 256 threads with three or four
-// chunks are slower (5120: 59 and 45; 8192: 83 and 44).
+// 82, 16384 61 and 62, 24000 90 and 112, both while threads past a row's end took
+// part in its last pass, 86 since).  In the forward pass 256 threads with three or
+// four chunks are slower (5120: 59 and 45; 8192: 83 and 44).
 template <typename T, bool BACKWARD, typename F>
 hipError_t norm_config(int64_t dim, F&& f) {
   using std::integral_constant;
